@@ -232,9 +232,10 @@ __device__ __forceinline__ void clear_heads(uint8_t* dst, int32_t G, int32_t per
   }
 }
 
-// 1 - 2 / (1 + e^2x): absolute error of a few 2^-24 over the whole range.
+// 1 - 2 / (1 + e^2x): absolute error of a few 2^-24 over the whole range.  NaN
+// stays NaN (fminf would give 40 for it).
 __device__ __forceinline__ float tanh_of(float x) {
-  return 1.0f - __fdividef(2.0f, 1.0f + tc::ex2(fminf(x, 40.0f) * (2.0f * LOG2E)));
+  return 1.0f - __fdividef(2.0f, 1.0f + tc::ex2((x > 40.0f ? 40.0f : x) * (2.0f * LOG2E)));
 }
 
 // Host side, shared by both directions.

@@ -1,0 +1,70 @@
+"""Attention over selected keys at the edges of its inputs: values that are not
+finite, very large or very small ones, rows with one key, clusters with several
+items, other streams.  64-bit references and bounds: tests/attention_reference.py."""
+import math
+
+import pytest
+import torch
+
+from tests import attention_reference as ref
+from tests.test_sparse_attention_gpu import _rand, _select, ets  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda", 0)
+# tokens: few (a row's items are shared by a cluster) and more than SMs
+TOKENS = [2, 400]
+
+
+def _inputs(T, H, Hk, D, K, S, dtype=torch.bfloat16, fill=None):
+    q, k, v = (_rand(s, dtype, i) for i, s in enumerate(((T, H, D), (S, Hk, D), (S, Hk, D))))
+    return q, k, v, _select(T, K, S, fill=fill)
+
+
+def _bad_head_and_key(T, H, D, dtype=torch.bfloat16):
+    """q with a NaN in head 1 of token 1 and k with one in a key that only token
+    0 selects."""
+    q, k, v, idx = _inputs(T, H, 1, D, 200, 500, dtype)
+    key = int(idx[0, 150])
+    idx[1:][idx[1:] == key] = -1
+    clean = q.clone(), k.clone()
+    q[1, 1, 7] = math.nan
+    k[key, 0, 3] = math.nan
+    return q, k, v, idx, key, clean
+
+
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("H", [4, 40, 100])
+def test_nan_scores_stay_nan(ets, softcap, T, H):  # noqa: F811
+    """Rows with a NaN score are NaN, with and without the cap; the others do not change."""
+    q, k, v, idx, key, clean = _bad_head_and_key(T, H, 64)
+    good = torch.ones((T, H), dtype=torch.bool, device=DEV)
+    good[1, 1] = False
+    good[0] = False
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, softcap=softcap, return_lse=True)
+    want, wlse = ets.topk_sparse_attention(*clean, v, idx, softcap=softcap, return_lse=True)
+    assert bool(out[~good].isnan().all()) and bool(lse[0].isnan().all())
+    assert torch.equal(out[good], want[good]) and torch.equal(lse[good], wlse[good])
+    dout = _rand(q.shape, q.dtype, 7)
+    bad_lse = wlse.clone()
+    bad_lse[~good] = math.nan
+    dq, dk, dv = ets.topk_sparse_attention_backward(dout, q, k, v, idx, out, bad_lse,
+                                                    softcap=softcap)
+    assert bool(dq[~good].isnan().all()) and bool(dq[good].isfinite().all())
+    hit = torch.zeros(500, dtype=torch.bool, device=DEV)
+    hit[idx[:2][idx[:2] >= 0].long()] = True
+    assert bool(dk[hit].isnan().all()) and bool(dv[hit].isnan().all())
+    assert bool(dk[~hit].isfinite().all()) and bool(dv[~hit].isfinite().all())
+
+
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("H", [4, 40, 100])
+def test_nan_scores_hidden_by_the_cap_in_the_gradient(ets, T, H):  # noqa: F811
+    """The scores alone carry the NaN (lse and out are the clean call's)."""
+    q, k, v, idx, key, clean = _bad_head_and_key(T, H, 64)
+    out, lse = ets.topk_sparse_attention(*clean, v, idx, softcap=5.0, return_lse=True)
+    dq, dk, _ = ets.topk_sparse_attention_backward(_rand(q.shape, q.dtype, 7), q, k, v, idx, out,
+                                                   lse, softcap=5.0)
+    assert bool(dq[1, 1].isnan().all()) and bool(dq[0].isnan().all())
+    assert bool(dk[key].isnan().all())
