@@ -311,7 +311,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
       __syncwarp();
       if (lane == 0) tc::bar_arrive(settled(wg, wq));
       if (own != ref) {
-        l = own == -INFINITY ? 0.0f : l * tc::ex2(own - ref);
+        // (with no finite maximum yet, l is 0, or NaN where all scores so far were:
+        // fmaxf drops them, and the sum has to keep them)
+        if (own != -INFINITY) l *= tc::ex2(own - ref);
         own = ref;
       }
       const float zero = ref == -INFINITY ? 0.0f : ref;
@@ -439,8 +441,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
         m = keep->ref[row];
 #pragma unroll
         for (int g = 0; g < 2; ++g)
-          if ((done.tiles > 1 || g == done.first) && keep->by[g][row] != -INFINITY)
-            l += keep->sum[g][row] * tc::ex2(keep->by[g][row] - m);
+          if (done.tiles > 1 || g == done.first) {
+            const float by = keep->by[g][row];
+            l += by == -INFINITY ? keep->sum[g][row] : keep->sum[g][row] * tc::ex2(by - m);
+          }
       }
       if (C == 1) {
         // the whole row into registers: O is free after a few hundred cycles, and

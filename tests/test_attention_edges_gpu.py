@@ -68,3 +68,19 @@ def test_nan_scores_hidden_by_the_cap_in_the_gradient(ets, T, H):  # noqa: F811
                                                    lse, softcap=5.0)
     assert bool(dq[1, 1].isnan().all()) and bool(dq[0].isnan().all())
     assert bool(dk[key].isnan().all())
+
+
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("H", [4, 40, 100])
+def test_log_sum_of_nan_scores_is_nan(ets, T, H):  # noqa: F811
+    """A head whose scores are all NaN has lse NaN: -inf means that no key is left."""
+    q, k, v, idx = _inputs(T, H, 1, 128, 300, 500)
+    want = ets.topk_sparse_attention(q, k, v, idx, return_lse=True)[1]
+    q[1, 1, 7] = math.nan
+    idx[0] = -1
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, return_lse=True)
+    assert bool(lse[1, 1].isnan()) and bool(out[1, 1].isnan().all())
+    assert bool((lse[0] == -math.inf).all()) and float(out[0].float().abs().max()) == 0.0
+    rest = torch.ones((T, H), dtype=torch.bool, device=DEV)
+    rest[0], rest[1, 1] = False, False
+    assert torch.equal(lse[rest], want[rest])
