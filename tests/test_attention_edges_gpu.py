@@ -12,7 +12,8 @@ from tests.test_sparse_attention_gpu import _rand, _select, ets  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 DEV = torch.device("cuda", 0)
-# tokens: few (a row's items are shared by a cluster) and more than SMs
+# tokens: few (with five chunks of keys and more, clusters share their items) and
+# more than SMs
 TOKENS = [2, 400]
 
 
@@ -24,7 +25,7 @@ def _inputs(T, H, Hk, D, K, S, dtype=torch.bfloat16, fill=None):
 def _bad_head_and_key(T, H, D, dtype=torch.bfloat16):
     """q with a NaN in head 1 of token 1 and k with one in a key that only token
     0 selects."""
-    q, k, v, idx = _inputs(T, H, 1, D, 200, 500, dtype)
+    q, k, v, idx = _inputs(T, H, 1, D, 600, 900, dtype)
     key = int(idx[0, 150])
     idx[1:][idx[1:] == key] = -1
     clean = q.clone(), k.clone()
@@ -52,7 +53,7 @@ def test_nan_scores_stay_nan(ets, softcap, T, H):  # noqa: F811
     dq, dk, dv = ets.topk_sparse_attention_backward(dout, q, k, v, idx, out, bad_lse,
                                                     softcap=softcap)
     assert bool(dq[~good].isnan().all()) and bool(dq[good].isfinite().all())
-    hit = torch.zeros(500, dtype=torch.bool, device=DEV)
+    hit = torch.zeros(900, dtype=torch.bool, device=DEV)
     hit[idx[:2][idx[:2] >= 0].long()] = True
     assert bool(dk[hit].isnan().all()) and bool(dv[hit].isnan().all())
     assert bool(dk[~hit].isfinite().all()) and bool(dv[~hit].isfinite().all())
@@ -74,7 +75,7 @@ def test_nan_scores_hidden_by_the_cap_in_the_gradient(ets, T, H):  # noqa: F811
 @pytest.mark.parametrize("H", [4, 40, 100])
 def test_log_sum_of_nan_scores_is_nan(ets, T, H):  # noqa: F811
     """A head whose scores are all NaN has lse NaN: -inf means that no key is left."""
-    q, k, v, idx = _inputs(T, H, 1, 128, 300, 500)
+    q, k, v, idx = _inputs(T, H, 1, 128, 600, 900)
     want = ets.topk_sparse_attention(q, k, v, idx, return_lse=True)[1]
     q[1, 1, 7] = math.nan
     idx[0] = -1
