@@ -105,6 +105,55 @@ struct Plan {
 };
 static_assert(Plan<128>::BYTES <= 232448 && Plan<64>::BYTES <= 232448, "shared memory plan");
 
+// Infinite values.  A weight above zero times an infinite value is that infinity,
+// but in the product such a value also meets weights that are zero (the other row
+// copies', or one that underflowed), and 0 * inf is NaN.  A result that is NaN
+// under a finite sum is therefore looked up in the values themselves: NaN or both
+// signs selected, it stays; else it is the infinity.  Only then is any of this
+// code run; without it a check of 64 instructions per row is left.
+//
+// One warp: of the 32 columns from c0 on, in which does a selected value of token
+// t, key head hk hold NaN, +inf, -inf (a bit per column each)?
+template <bool BF16>
+__device__ __forceinline__ void value_kinds(const Args& a, int32_t t, int32_t hk, uint32_t c0,
+                                            uint32_t lane, uint32_t (&kinds)[3]) {
+  constexpr uint32_t INF = BF16 ? 0x7f80u : 0x7c00u;
+  const int32_t* idx = a.idx + (int64_t)t * a.ld_idx;
+  const int32_t lo = a.lo ? max(a.lo[t], 0) : 0, hi = a.hi ? min(a.hi[t], a.S) : a.S;
+  kinds[0] = kinds[1] = kinds[2] = 0u;
+#pragma unroll 1
+  for (int64_t j = lane; j < a.K; j += 32) {
+    const int32_t i = idx[j];
+    if (i < lo || i >= hi) continue;
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) +
+                                                          i * a.v_ts + hk * a.v_hs + c0 * 2u);
+#pragma unroll 4
+    for (uint32_t w = 0; w < 16; ++w) {
+      const uint32_t two = __ldg(v + w);
+#pragma unroll
+      for (uint32_t s = 0; s < 2; ++s) {
+        const uint32_t x = s ? two >> 16 : two & 0xffffu, bit = 1u << (2 * w + s);
+        if ((x & 0x7fffu) > INF) kinds[0] |= bit;
+        else if (x == INF) kinds[1] |= bit;
+        else if (x == (0x8000u | INF)) kinds[2] |= bit;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) kinds[k] = __reduce_or_sync(0xffffffffu, kinds[k]);
+}
+// The result x of column c0 + column; `none`: the row's sum is zero.
+template <bool BF16>
+__device__ __forceinline__ uint16_t looked_up(uint16_t x, const uint32_t (&kinds)[3],
+                                              uint32_t column, bool none) {
+  constexpr uint32_t INF = BF16 ? 0x7f80u : 0x7c00u;
+  if ((x & 0x7fffu) <= INF) return x;
+  if (none) return 0;
+  const bool pos = kinds[1] >> column & 1u, neg = kinds[2] >> column & 1u;
+  if ((kinds[0] >> column & 1u) || pos == neg) return x;
+  return (uint16_t)(pos ? INF : 0x8000u | INF);
+}
+
 // NC: key columns of a tile per row copy (128 / copies).  BENT: a cap or a bias.
 // Chunks of 32 columns run in loops, not unrolled: five kinds of warps share the
 // instruction cache, and 64 columns held in registers took longer than 32 read
@@ -512,16 +561,39 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
           }
           if (!ok) break;
         }
+        bool odd = false;  // something is not finite although the sum is
+        uint16_t* mine = static_cast<uint16_t*>(a.out) + ((int64_t)t * a.H + hk * a.G + h) * D;
         if (copy == 0 && (int32_t)h < a.G) {
-          const int64_t at = (int64_t)t * a.H + hk * a.G + h;
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D);
+          uint4* dst = reinterpret_cast<uint4*>(mine);
+          uint64_t none2 = 0ull;
 #pragma unroll
-          for (int k = 0; k < D; k += 8)
+          for (int k = 0; k < D; k += 8) {
             dst[k / 8] = make_uint4(
                 tc::pack16<BF16>(o[k], o[k + 1]), tc::pack16<BF16>(o[k + 2], o[k + 3]),
                 tc::pack16<BF16>(o[k + 4], o[k + 5]), tc::pack16<BF16>(o[k + 6], o[k + 7]));
+#pragma unroll
+            for (int i = 0; i < 8; i += 2)
+              none2 = tc::fma2(tc::pack2(o[k + i], o[k + i + 1]), 0ull, none2);
+          }
           if (a.lse)
-            a.lse[at] = lh != 0.0f ? (zero + log2f(lh)) * 0.6931471805599453f : -INFINITY;
+            a.lse[(int64_t)t * a.H + hk * a.G + h] =
+                lh != 0.0f ? (zero + log2f(lh)) * 0.6931471805599453f : -INFINITY;
+          float n0, n1;
+          tc::unpack2(none2, &n0, &n1);
+          odd = n0 + n1 != 0.0f && lh == lh;
+        }
+        if (__any_sync(0xffffffffu, odd)) {
+          asm volatile("" ::: "memory");  // the row is read back
+#pragma unroll 1
+          for (uint32_t c0 = 0; c0 < (uint32_t)D; c0 += 32) {
+            uint32_t kinds[3];
+            value_kinds<BF16>(a, t, hk, c0, lane, kinds);
+            if (odd) {
+#pragma unroll 1
+              for (uint32_t i = 0; i < 32; ++i)
+                mine[c0 + i] = looked_up<BF16>(mine[c0 + i], kinds, i, lh == 0.0f);
+            }
+          }
         }
         continue;
       }
@@ -609,6 +681,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
         // the joined rows, 4 elements per thread and step
 #pragma unroll 1
         for (uint32_t q = spare ? 0u : part; q <= part; ++q) {
+          float none = 0.0f;
 #pragma unroll 1
           for (uint32_t e = rank * 128u + (tid & 127u); e < (uint32_t)a.G * 8u; e += C * 128u) {
             const uint32_t hh = e >> 3, p = e & 7u;
@@ -633,6 +706,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
             uint16_t* dst = static_cast<uint16_t*>(a.out) +
                             ((int64_t)t * a.H + hk * a.G + hh) * D + q * 32 + p * 4;
             *reinterpret_cast<uint2*>(dst) = w;
+            none = fmaf(x.x, 0.0f, fmaf(x.y, 0.0f, fmaf(x.z, 0.0f, fmaf(x.w, 0.0f, none))));
+          }
+          if (__any_sync(0xffffffffu, none != 0.0f)) {
+            asm volatile("" ::: "memory");  // the elements are read back
+            uint32_t kinds[3];
+            value_kinds<BF16>(a, t, hk, q * 32u, lane, kinds);
+#pragma unroll 1
+            for (uint32_t e = rank * 128u + (tid & 127u); e < (uint32_t)a.G * 8u; e += C * 128u) {
+              const uint32_t hh = e >> 3, p = e & 7u;
+              float sum = 0.0f;
+              for (uint32_t c = 0; c < C; ++c) sum += wt[c * 128 + hh];
+              if (sum != sum) continue;
+              uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                              ((int64_t)t * a.H + hk * a.G + hh) * D + q * 32 + p * 4;
+#pragma unroll 1
+              for (uint32_t i = 0; i < 4; ++i)
+                dst[i] = looked_up<BF16>(dst[i], kinds, p * 4 + i, sum == 0.0f);
+            }
           }
         }
         // everybody has read the rows (the last ones stay until the cluster leaves)

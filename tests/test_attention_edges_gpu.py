@@ -22,6 +22,13 @@ def _inputs(T, H, Hk, D, K, S, dtype=torch.bfloat16, fill=None):
     return q, k, v, _select(T, K, S, fill=fill)
 
 
+def _same_kind(got, want):
+    """Equal where want is not finite (NaN with NaN, infinities by sign)."""
+    got, want = got.double(), want.double()
+    kind = lambda x: torch.where(x.isnan(), 2.0, torch.where(x.isinf(), x.sign(), 0.0))  # noqa: E731
+    return torch.equal(kind(got), kind(want))
+
+
 def _bad_head_and_key(T, H, D, dtype=torch.bfloat16):
     """q with a NaN in head 1 of token 1 and k with one in a key that only token
     0 selects."""
@@ -85,3 +92,35 @@ def test_log_sum_of_nan_scores_is_nan(ets, T, H):  # noqa: F811
     rest = torch.ones((T, H), dtype=torch.bool, device=DEV)
     rest[0], rest[1, 1] = False, False
     assert torch.equal(lse[rest], want[rest])
+
+
+def _infinite_values(v, keys):
+    """Infinities and NaN in columns of their own: one +inf, one -inf, two +inf,
+    both signs, a NaN, a NaN beside an infinity."""
+    a, b = (int(x) for x in keys)
+    v[a, :, 0] = math.inf
+    v[b, :, 1] = -math.inf
+    v[a, :, 2], v[b, :, 2] = math.inf, math.inf
+    v[a, :, 3], v[b, :, 3] = math.inf, -math.inf
+    v[a, :, 4] = math.nan
+    v[a, :, 5], v[b, :, 5] = math.inf, math.nan
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", TOKENS + [160])
+@pytest.mark.parametrize("H,Hk,D", [(4, 1, 64), (40, 1, 128), (100, 1, 64), (16, 2, 128)])
+def test_infinite_values(ets, dtype, T, H, Hk, D):  # noqa: F811
+    """A selected infinity gives an infinity, however many heads share the key and
+    however small its weight; keys a and b lie in different tiles and parts of them."""
+    K, S = (2048, 3000) if T == 160 else (600, 900)  # 160 items: clusters with several each
+    q, k, v, idx = _inputs(T, H, Hk, D, K, S, dtype)
+    _infinite_values(v, (idx[0, 5], idx[0, 450]))
+    idx[1, :] = idx[0]  # a second row with both
+    q[1] *= 8           # whose weights are far apart
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, return_lse=True)
+    n = min(T, 24)
+    r = ref.attend(q[:n], k, v, idx[:n], D ** -0.5)
+    assert _same_kind(out[:n], r["out"]) and bool(lse.isfinite().all())
+    bound, _ = ref.attend_bounds(r, v, idx[:n], dtype)
+    fine = r["out"].isfinite()
+    assert bool(((out[:n].double() - r["out"]).abs() <= bound)[fine].all())
