@@ -73,6 +73,58 @@ __device__ __forceinline__ void red4(float* p, float4 v) {
                : "memory");
 }
 
+// Infinite output gradients.  P is zero in the other copies' keys, and 0 * inf makes
+// their part of dV NaN, where p * inf is that infinity.  So NaN in four neighbouring
+// columns (from col on) of dV of token t, key head hk is looked up in the heads' dout:
+// NaN or both signs there, it stays; else it is the infinity.  A head without a key
+// (lse = -inf) takes no part; where a head's weights are NaN (lse is not finite) all
+// stays.  Bits 0..3, 4..7: which columns become +inf, -inf.
+template <bool BF16>
+__device__ __forceinline__ uint32_t infinite_columns(const Args& a, int32_t t, int32_t hk,
+                                                     uint32_t col) {
+  constexpr uint32_t INF = BF16 ? 0x7f80u : 0x7c00u;
+  uint32_t nan = 0u, pos = 0u, neg = 0u;
+#pragma unroll 1
+  for (int32_t h = hk * a.G; h < (hk + 1) * a.G; ++h) {
+    const float lse = a.lse_in[(int64_t)t * a.H + h];
+    if (lse == -INFINITY) continue;
+    if (!(fabsf(lse) < INFINITY)) return 0u;
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.dout) +
+                                                    t * a.do_ts + h * a.do_hs + col * 2u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t two = i < 2 ? w.x : w.y, x = i & 1 ? two >> 16 : two & 0xffffu;
+      nan |= (uint32_t)((x & 0x7fffu) > INF) << i;
+      pos |= (uint32_t)(x == INF) << i;
+      neg |= (uint32_t)(x == (0x8000u | INF)) << i;
+    }
+  }
+  return (pos & ~neg & ~nan) | (neg & ~pos & ~nan) << 4;
+}
+// The staged rows of a chunk of dV to the sums, such NaN replaced.  Not inlined: any
+// code among the usual rows' loads and reductions costs them (568 us for 490 with
+// 1024 x 64 heads x 128), although it never runs.
+template <int D, bool BF16>
+__device__ __noinline__ void add_odd_rows(const Args* a, int32_t t, int32_t hk, uint32_t c,
+                                          uint32_t wq, uint32_t lane, const Tile* tile,
+                                          const float* stage, float* sum) {
+  const int64_t key_floats = (int64_t)a->Hk * D;
+  const uint32_t inf = infinite_columns<BF16>(*a, t, hk, c + (lane & 7u) * 4u);
+  auto put = [&](float& v, uint32_t i) {
+    if (v != v && (inf >> i & 1u)) v = INFINITY;
+    if (v != v && (inf >> (4 + i) & 1u)) v = -INFINITY;
+  };
+#pragma unroll 1
+  for (uint32_t r = wq * 32u + (lane >> 3); r < wq * 32u + 32u; r += 4) {
+    float4 x = *reinterpret_cast<const float4*>(stage + r * 32 + (((lane & 7u) ^ (r & 7u)) << 2));
+    put(x.x, 0);
+    put(x.y, 1);
+    put(x.z, 2);
+    put(x.w, 3);
+    if ((int32_t)r < tile->count) red4(sum + tile->key[r] * key_floats, x);
+  }
+}
+
 template <int D, int NC, bool BF16>
 __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_constant__ Args a) {
   using P = GradPlan<D>;
@@ -245,6 +297,11 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
     for (int32_t item = first; item < a.items && ok; item += step) {
       const int32_t t = item / a.Hk, hk = item - t * a.Hk;
       bool any = false;
+      // an infinite or NaN dout leaves its mark in delta; without one dV needs no look
+      // (looking at every row of dV took 615 us for 493 with 1024 x 64 heads x 128)
+      bool mark = false;
+      for (int32_t h = (int32_t)lane; h < a.G; h += 32)
+        mark |= !(fabsf(a.delta[(int64_t)t * a.H + hk * a.G + h]) < INFINITY);
       for (;;) {
         const uint32_t is = ti % G_NI;
         if (!wait_warp(ix_full(is), (ti / G_NI) & 1u)) { ok = false; break; }
@@ -263,6 +320,7 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
             const uint32_t b = e % 3u;
             if (!wait_warp(acc_full(b), (e / 3u) & 1u)) { ok = false; break; }
             tc::fence_after();
+            const bool odd = __any_sync(0xffffffffu, mark) && !(e & 1u);
             float* sum = ((e & 1u) ? a.dk32 : a.dv32) + (int64_t)hk * D + (lane & 7u) * 4u;
             const float f = (e & 1u) ? a.scale : 1.0f;
 #pragma unroll 1
@@ -281,6 +339,10 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
                 *reinterpret_cast<float4*>(stage + row * 32 + (((i >> 2) ^ (row & 7u)) << 2)) =
                     make_float4(u[i] * f, u[i + 1] * f, u[i + 2] * f, u[i + 3] * f);
               __syncwarp();
+              if (odd) {
+                add_odd_rows<D, BF16>(&a, t, hk, c, wq, lane, tile, stage, sum + c);
+                continue;
+              }
               // four rows of 128 bytes per step; the reads of all eight steps first
               // (each waited for the one before it when they took turns)
               float4 x[8];

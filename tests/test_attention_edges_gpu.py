@@ -124,3 +124,29 @@ def test_infinite_values(ets, dtype, T, H, Hk, D):  # noqa: F811
     bound, _ = ref.attend_bounds(r, v, idx[:n], dtype)
     fine = r["out"].isfinite()
     assert bool(((out[:n].double() - r["out"]).abs() <= bound)[fine].all())
+
+
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("H,Hk,D", [(4, 1, 64), (40, 1, 128), (100, 1, 64), (16, 2, 128)])
+def test_infinite_output_gradients(ets, T, H, Hk, D):  # noqa: F811
+    """dv of an infinite dout is infinite (with its sign), NaN where both signs or a NaN meet."""
+    K, S = 200, 300
+    q, k, v, idx = _inputs(T, H, Hk, D, K, S)
+    dout = _rand(q.shape, q.dtype, 7)
+    dout[0, 0, 0] = math.inf
+    dout[1, H - 1, 1] = -math.inf
+    dout[0, 0, 2], dout[1, 1, 2] = math.inf, -math.inf
+    dout[1, 0, 3] = math.nan
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, return_lse=True)
+    n = 2
+    got = ets.topk_sparse_attention_backward(dout[:n].contiguous(), q[:n].contiguous(), k, v,
+                                             idx[:n].contiguous(), out[:n].contiguous(),
+                                             lse[:n].contiguous())
+    r = ref.attend(q[:n], k, v, idx[:n], D ** -0.5)
+    want, bound = ref.attend_grad(dout[:n], q[:n], k, v, idx[:n], out[:n], lse[:n], r, D ** -0.5)
+    assert _same_kind(got[2], want[2])
+    fine = want[2].isfinite() & bound[2].isfinite()
+    assert bool(((got[2].double() - want[2]).abs() <= bound[2])[fine].all())
+    if T > n:  # the other tokens' rows of the whole call
+        dq = ets.topk_sparse_attention_backward(dout, q, k, v, idx, out, lse)[0]
+        assert bool(dq[n:].isfinite().all())
