@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
         own = -INFINITY;
         l = 0.0f;
         if (BENT && a.slopes) {
-          const int32_t t = tile->token, hk = tile->head;
+          const int32_t t = tile->token, hk = tile->mark;
           slope = (int32_t)h < a.G ? a.slopes[hk * a.G + h] * LOG2E : 0.0f;
           pos = a.pos[t];
         }
@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
       // --------------------------------------------------------- index rows
       uint32_t ti = 0;
       compact_rows(
-          a, first, step, (int32_t)rank, (int32_t)C, lane,
+          a, first, step, (int32_t)rank, (int32_t)C, lane, [](int32_t, int32_t hk) { return hk; },
           [&]() -> Tile* {
             return wait_warp(ix_empty(ti % NI), ((ti / NI) & 1u) ^ 1u) ? tiles + ti % NI : nullptr;
           },

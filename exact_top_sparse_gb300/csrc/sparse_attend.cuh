@@ -46,7 +46,8 @@ struct Tile {
   int32_t key[KT];
   int32_t count;
   int32_t last;                        // 1: the item's last tile
-  int32_t token, head;                 // the item
+  int32_t token;                       // the item's
+  int32_t mark;                        // forward: its key head; gradient: dS's factor (bits)
 };
 
 // 16-byte piece `piece` of row `row` in a tile of 128-byte swizzled rows, one
@@ -60,14 +61,15 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t row, uint32_t piece, uint3
 // anything outside the token's key range is dropped, so a masked key is neither
 // read nor multiplied.  Every item gives at least one tile (count 0 where nothing
 // is left).
-//   acquire() -> Tile* (nullptr: gave up), publish() hands it over.
+//   acquire() -> Tile* (nullptr: gave up), publish() hands it over; mark(token, key
+//   head) -> the item's Tile::mark, called by the whole warp.
 // A lane takes four neighbouring entries (one 16-byte load where rows allow it),
 // and two chunks are on their way while one is compacted, across items: with
 // single loads, one chunk ahead, this warp took 1500 cycles a tile, more than the
 // products.
-template <class Acquire, class Publish>
+template <class Mark, class Acquire, class Publish>
 __device__ __forceinline__ void compact_rows(const Args& a, int32_t first, int32_t istep,
-                                             int32_t c0, int32_t cstep, uint32_t lane,
+                                             int32_t c0, int32_t cstep, uint32_t lane, Mark mark,
                                              Acquire acquire, Publish publish) {
   struct Chunk {
     int4 v;
@@ -110,7 +112,7 @@ __device__ __forceinline__ void compact_rows(const Args& a, int32_t first, int32
   Chunk next = load();
   Chunk after = load();
   for (int32_t item = first; item < a.items; item += istep) {
-    const int32_t t = item / a.Hk, hk = item - t * a.Hk;
+    const int32_t t = item / a.Hk, its_mark = mark(t, item - t * a.Hk);
     Tile* tile = acquire();
     if (!tile) return;
     int32_t n = 0;
@@ -119,7 +121,7 @@ __device__ __forceinline__ void compact_rows(const Args& a, int32_t first, int32
         tile->count = last ? n : KT;
         tile->last = last;
         tile->token = t;
-        tile->head = hk;
+        tile->mark = its_mark;
       }
       publish();
     };

@@ -20,8 +20,13 @@
 // them 341 us at that rate).  Without the reductions a tile takes 6700 cycles
 // instead of 8400, without their way through tensor and shared memory 6000.  Their
 // order is the scheduler's, so the sums differ by FP32 rounding between runs.
-// dS leaves the scale out until the FP32 results, so that FP16 keeps more of
-// its range for small weights.
+// P and dS are rounded to the inputs' 16-bit type before the last three products
+// (the tensor core takes no wider operand beside 16-bit values; the error against
+// 64 bits is 1.1 to 1.4 times that of FP32 products).  dS leaves the scale out until
+// the FP32 results, and in FP16 it is held times a power of two that brings the
+// item's largest |dout| into [4, 8) and is taken out of those results, exactly: with a
+// scaled loss dS itself passes 65504 where dq, dk and dv do not.  8 (|v|_1 + |out|_1)
+// bounds it then: finite for values whose absolute sum over D is below 4094.
 //
 // Tried and slower: twice the draining warps (8900 cycles a tile), dV and dK in
 // halves of 64 columns with S and dP ahead of them (9400), bulk reductions of
@@ -125,6 +130,25 @@ __device__ __noinline__ void add_odd_rows(const Args* a, int32_t t, int32_t hk, 
   }
 }
 
+// One warp: the power of two that brings the largest |dout| of an item into [4, 8)
+// (1 where there is none, or one that is not finite), as the bits of a float.
+template <int D>
+__device__ __forceinline__ int32_t factor_bits(const Args& a, int32_t t, int32_t hk, uint32_t lane) {
+  constexpr uint32_t PIECES = D / 8;
+  const uint8_t* src = static_cast<const uint8_t*>(a.dout) + t * a.do_ts + (int64_t)hk * a.G * a.do_hs;
+  uint32_t top = 0u;  // largest magnitudes of the even and the odd elements
+#pragma unroll 8
+  for (uint32_t e = lane; e < (uint32_t)a.G * PIECES; e += 32) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + (e / PIECES) * a.do_hs + e % PIECES * 16));
+    top = __vmaxu2(__vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu)),
+                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  }
+  const uint32_t m = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+  if (m == 0u || m >= 0x7c00u) return __float_as_int(1.0f);
+  const int32_t exponent = (__float_as_int(__half2float(__ushort_as_half((uint16_t)m))) >> 23) - 127;
+  return (127 + 2 - exponent) << 23;
+}
+
 template <int D, int NC, bool BF16>
 __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_constant__ Args a) {
   using P = GradPlan<D>;
@@ -217,6 +241,7 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
           tc::fence_after();
           const uint32_t ts = tmem + lanes + ((2u * n) % 3u) * 128u + col0;
           const uint32_t td = tmem + lanes + ((2u * n + 1u) % 3u) * 128u + col0;
+          const float times = BF16 ? 1.0f : __int_as_float(tile->mark), less = -delta * times;
 #pragma unroll 1
           for (int c = 0; c < NC; c += 32) {
             float us[32], ud[32];
@@ -230,13 +255,13 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
                 const float th = tanh_of(us[i] * cap_in);
                 x[i] = cap_out * th;
                 // the cap's derivative goes with dP - delta
-                ud[i] = (ud[i] - delta) * fmaf(-th, th, 1.0f);
+                ud[i] = fmaf(ud[i], times, less) * fmaf(-th, th, 1.0f);
               }
             } else {
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 x[i] = us[i] * sc;
-                ud[i] -= delta;
+                ud[i] = fmaf(ud[i], times, less);
               }
             }
             if (a.slopes) {
@@ -297,6 +322,7 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
     for (int32_t item = first; item < a.items && ok; item += step) {
       const int32_t t = item / a.Hk, hk = item - t * a.Hk;
       bool any = false;
+      float undo = a.scale;  // dS's factor out of the results, and the scale in
       // an infinite or NaN dout leaves its mark in delta; without one dV needs no look
       // (looking at every row of dV took 615 us for 493 with 1024 x 64 heads x 128)
       bool mark = false;
@@ -308,6 +334,8 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
         const Tile* tile = tiles + is;
         const int32_t count = tile->count, last = tile->last;
         if (count > 0) {
+          if (!BF16)  // the factor's inverse: a power of two
+            undo = a.scale * __int_as_float((254 << 23) - tile->mark);
           // this lane's eight keys: row k * 4 + lane / 8 of the warp's 32
           int32_t key[8];
 #pragma unroll
@@ -322,7 +350,7 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
             tc::fence_after();
             const bool odd = __any_sync(0xffffffffu, mark) && !(e & 1u);
             float* sum = ((e & 1u) ? a.dk32 : a.dv32) + (int64_t)hk * D + (lane & 7u) * 4u;
-            const float f = (e & 1u) ? a.scale : 1.0f;
+            const float f = (e & 1u) ? undo : 1.0f;
 #pragma unroll 1
             for (uint32_t c = 0; c < (uint32_t)D; c += 32) {
               float u[32];
@@ -406,8 +434,8 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
             o.w += x.w;
           }
           uint2 w;
-          w.x = tc::pack16<BF16>(o.x * a.scale, o.y * a.scale);
-          w.y = tc::pack16<BF16>(o.z * a.scale, o.w * a.scale);
+          w.x = tc::pack16<BF16>(o.x * undo, o.y * undo);
+          w.y = tc::pack16<BF16>(o.z * undo, o.w * undo);
           uint16_t* dst = static_cast<uint16_t*>(a.dq) +
                           ((int64_t)t * a.H + hk * a.G + hh) * D + c + p * 4;
           *reinterpret_cast<uint2*>(dst) = w;
@@ -534,6 +562,7 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
       uint32_t ti = 0;
       compact_rows(
           a, first, step, 0, 1, lane,
+          [&](int32_t t, int32_t hk) { return BF16 ? 0 : factor_bits<D>(a, t, hk, lane); },
           [&]() -> Tile* {
             return wait_warp(ix_empty(ti % G_NI), ((ti / G_NI) & 1u) ^ 1u) ? tiles + ti % G_NI
                                                                            : nullptr;

@@ -506,7 +506,10 @@ int topk_sparse_attention_read_status(struct CUstream_st* stream, uint32_t* flag
  * where a key is in no row).  dk and dv are summed over the tokens and heads in
  * FP32 and rounded once; the order of the sums is not fixed, so they may differ
  * in the last bit between runs.  dq does not depend on the run.  There is no
- * gradient for slopes.
+ * gradient for slopes.  P and dS are rounded to the 16-bit type for the products
+ * that give dq, dk and dv; FP16 dS is held times a power of two by the size of the
+ * token's dout, and stays finite while the absolute values of a selected row of v
+ * sum to less than 4094.
  *   workspace  device, 16-byte aligned, topk_sparse_attention_backward_-
  *              workspace_bytes() bytes, not initialised
  * Three launches on `stream`. */

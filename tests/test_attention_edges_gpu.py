@@ -150,3 +150,34 @@ def test_infinite_output_gradients(ets, T, H, Hk, D):  # noqa: F811
     if T > n:  # the other tokens' rows of the whole call
         dq = ets.topk_sparse_attention_backward(dout, q, k, v, idx, out, lse)[0]
         assert bool(dq[n:].isfinite().all())
+
+
+@pytest.mark.parametrize("power", [-12, -4, 10, 12, 13])
+@pytest.mark.parametrize("H,Hk,D", [(2, 1, 128), (8, 2, 128), (36, 1, 64)])
+def test_float16_gradients_of_scaled_losses(ets, power, H, Hk, D):  # noqa: F811
+    """dout times 2^power: P (dP - delta) passes float16's 65504 where dq, dk and dv
+    do not.  dS is held times a power of two that puts the token's largest |dout|
+    into [4, 8), so what its rounding may lose below the normal range is
+    2^-25 / factor."""
+    T, K, S = 5, 40, 400
+    q = _rand((T, H, D), torch.float16, 1, 2.0)
+    k, v = _rand((S, Hk, D), torch.float16, 2, 1.5), _rand((S, Hk, D), torch.float16, 3, 3.0)
+    idx = _select(T, K, S)
+    dout = (_rand((T, H, D), torch.float32, 4).clamp(-3, 3) * 2.0 ** power).half()
+    scale = D ** -0.5
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, scale=scale, return_lse=True)
+    got = ets.topk_sparse_attention_backward(dout, q, k, v, idx, out, lse, scale=scale)
+    r = ref.attend(q, k, v, idx, scale)
+    want, bound = ref.attend_grad(dout, q, k, v, idx, out, lse, r, scale)
+    G = H // Hk
+    top = dout.double().abs().view(T, Hk, -1).amax(-1)  # [T, Hk]
+    lost = 2.0 ** -25 * 2.0 ** (torch.floor(torch.log2(top)) - 2)
+    i = idx.long()
+    bound[0] += scale * torch.einsum("tn,tknd->tnd", lost, k.double().abs()[i]).repeat_interleave(G, 1)
+    heads = q.double().abs().view(T, Hk, G, D).sum(2) * lost[..., None]
+    bound[1].index_add_(0, i.flatten(), scale * heads[:, None].expand(-1, K, -1, -1).reshape(-1, Hk, D))
+    for g, w, b in zip(got, want, bound):
+        keep = w.abs() < 65000  # what float16 holds
+        assert float(keep.double().mean()) > 0.99
+        err = (g.double() - w).abs()
+        assert bool((err <= b)[keep].all()), float((err / b)[keep].max())
