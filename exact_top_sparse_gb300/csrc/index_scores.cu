@@ -38,6 +38,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "per_device.h"
 #include "topk.h"
 #include "topk_device.cuh"
 #include "topk_launch.h"
@@ -602,13 +603,12 @@ int launch_index_scores(const uint16_t* q, const uint16_t* k, const float* w, in
   if (units > INT32_MAX) return TOPK_ERR_ARG;
   a.n_units = (int32_t)units;
   a.rows = rows;
-  static std::once_flag attr_once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once, [] {
-    attr_err = cudaFuncSetAttribute(k_index_scores, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)SMEM_BYTES);
-  });
-  if (attr_err != cudaSuccess) return TOPK_ERR_CUDA;
+  static OncePerDevice opted_in;
+  if (!opted_in.ensure(dev, [] {
+        return cudaFuncSetAttribute(k_index_scores, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)SMEM_BYTES) == cudaSuccess;
+      }))
+    return TOPK_ERR_CUDA;
   const int grid = (int)(units < sms ? units : sms);
   k_index_scores<<<grid, THREADS, SMEM_BYTES, stream>>>(mk, mq, a);
   return cudaGetLastError() == cudaSuccess ? TOPK_OK : TOPK_ERR_CUDA;

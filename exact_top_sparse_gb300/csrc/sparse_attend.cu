@@ -50,10 +50,10 @@
 // With few items a cluster of 2, 4 or 8 CTAs shares an item: CTA c takes the
 // 128-entry chunks c, c + C, ... of the index row; the partial results are
 // joined through distributed shared memory in a fixed order.
+#include "per_device.h"
 #include "sparse_attend.cuh"
 
 #include <cmath>
-#include <mutex>
 
 namespace ta {
 
@@ -934,13 +934,15 @@ int check_args(const Args& a, int32_t D, int32_t dtype) {
 
 template <int D, int NC, bool BF16, bool BENT>
 int launch_kernel(const Args& a, int C, int sms, cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(k_attend<D, NC, BF16, BENT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)Plan<D>::BYTES);
-  });
-  if (err != cudaSuccess) return TOPK_ERR_CUDA;
+  static OncePerDevice opted_in;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return TOPK_ERR_NO_DEVICE;
+  if (!opted_in.ensure(dev, [] {
+        return cudaFuncSetAttribute(k_attend<D, NC, BF16, BENT>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)Plan<D>::BYTES) == cudaSuccess;
+      }))
+    return TOPK_ERR_CUDA;
   const int clusters = a.items < sms / C ? a.items : sms / C;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(clusters * C));

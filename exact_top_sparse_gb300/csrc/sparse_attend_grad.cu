@@ -41,9 +41,8 @@
 //   16     tensor core; 17 index rows; 18 the items' q and dout heads
 // Tensor memory: three rotating buffers of 128 columns and dQ.  S(n) and dP(n)
 // take the next two; once P and dS are written, dV(n) and dK(n) replace them.
+#include "per_device.h"
 #include "sparse_attend.cuh"
-
-#include <mutex>
 
 namespace ta {
 
@@ -656,14 +655,15 @@ __global__ void __launch_bounds__(256) k_grad_end(const float4* dk32, const floa
 // ------------------------------------------------------------------ host side
 template <int D, int NC, bool BF16>
 int launch_grad(const Args& a, int sms, cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(k_attend_grad<D, NC, BF16>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)GradPlan<D>::BYTES);
-  });
-  if (err != cudaSuccess) return TOPK_ERR_CUDA;
+  static OncePerDevice opted_in;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return TOPK_ERR_NO_DEVICE;
+  if (!opted_in.ensure(dev, [] {
+        return cudaFuncSetAttribute(k_attend_grad<D, NC, BF16>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)GradPlan<D>::BYTES) == cudaSuccess;
+      }))
+    return TOPK_ERR_CUDA;
   const int grid = a.items < sms ? a.items : sms;
   k_attend_grad<D, NC, BF16><<<grid, G_THREADS, GradPlan<D>::BYTES, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? TOPK_OK : TOPK_ERR_CUDA;
