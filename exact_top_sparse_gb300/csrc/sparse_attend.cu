@@ -34,10 +34,11 @@
 //          values) into tensor memory.  The groups share each row's reference
 //          maximum: a group settles its tile's before the other settles the
 //          next one's.  It changes, and the accumulator is rescaled, only when
-//          a maximum rises above it by more than 2^64 (BF16) or 2^15 (FP16:
+//          a maximum rises above it by more than 2^32 (BF16) or 2^15 (FP16:
 //          P < 65504); a rescale stalls both groups and the tensor core, and at
 //          2^8 sharp heads (logits of standard deviation 4) took 1.6 times as
-//          long as flat ones
+//          long as flat ones.  In BF16 P is held 2^32 times smaller, so that it
+//          never passes 1: sums overflow only where the values' own sum would
 //   8..15  gather: cp.async of 16-byte pieces into rings of swizzled tiles,
 //          four warps for the keys, four for the values
 //   16..19 the finished items: O from tensor memory, joined and written, while
@@ -181,8 +182,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
   constexpr int PER = NC;  // rows per copy: with R = 128 / NC copies, 128 / R rows
   constexpr int COPIES = 128 / PER;
   // how far (base 2) a maximum may rise above its row's reference: P and the FP32
-  // sums have the exponents for it, a relative error does not depend on them
-  constexpr float GROWTH = BF16 ? 64.0f : 15.0f;
+  // sums have the exponents for it, a relative error does not depend on them.  What
+  // P is held smaller by: FP16 has no exponents to spare below, and its values do
+  // not reach the end of FP32
+  constexpr float GROWTH = BF16 ? 32.0f : 15.0f, SMALLER = BF16 ? 32.0f : 0.0f;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::saddr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
         if (own != -INFINITY) l *= tc::ex2(own - ref);
         own = ref;
       }
-      const float zero = ref == -INFINITY ? 0.0f : ref;
+      const float zero = ref == -INFINITY ? 0.0f : ref + SMALLER;
       const uint64_t mul2 = tc::pack2(mul, mul), zero2 = tc::pack2(-zero, -zero);
       uint64_t l2 = 0ull;
       auto weigh = [&](const float (&x)[32], int at) {
@@ -594,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
           }
           if (a.lse)
             a.lse[(int64_t)t * a.H + hk * a.G + h] =
-                lh != 0.0f ? (zero + log2f(lh)) * 0.6931471805599453f : -INFINITY;
+                lh != 0.0f ? (zero + SMALLER + log2f(lh)) * 0.6931471805599453f : -INFINITY;
           float n0, n1;
           tc::unpack2(none2, &n0, &n1);
           odd = n0 + n1 != 0.0f && lh == lh;
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
             if (c < C && copy == 0) wt[c * 128 + h] = mc[c] * inv;
           if (a.lse && rank == 0 && copy == 0 && (int32_t)h < a.G)
             a.lse[(int64_t)t * a.H + hk * a.G + h] =
-                sum != 0.0f ? (zero + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                sum != 0.0f ? (zero + SMALLER + log2f(sum)) * 0.6931471805599453f : -INFINITY;
           if (!here()) { ok = false; break; }
         }
         // the joined rows, 4 elements per thread and step

@@ -181,3 +181,24 @@ def test_float16_gradients_of_scaled_losses(ets, power, H, Hk, D):  # noqa: F811
         assert float(keep.double().mean()) > 0.99
         err = (g.double() - w).abs()
         assert bool((err <= b)[keep].all()), float((err / b)[keep].max())
+
+
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("H", [4, 40, 100])
+@pytest.mark.parametrize("power", [75, -60])
+def test_large_and_small_values_under_growing_scores(ets, T, H, power):  # noqa: F811
+    """Values near 2^power in bfloat16 while the scores' maximum climbs by 20 nats
+    a tile: weights and values together stay inside FP32."""
+    D, S = 64, 768
+    q = _rand((T, H, D), torch.bfloat16, 4, 0.05)
+    q[..., 0] = 1.0
+    k = _rand((S, 1, D), torch.bfloat16, 5, 0.05)
+    k[:, 0, 0] = torch.tensor([0.0, 20, 40], device=DEV).repeat_interleave(256).bfloat16()
+    v = (_rand((S, 1, D), torch.float32, 6) * 2.0 ** power).bfloat16()
+    idx = torch.arange(S, dtype=torch.int32, device=DEV)[None].repeat(T, 1)
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, scale=1.0, return_lse=True)
+    n = 4
+    r = ref.attend(q[:n], k, v, idx[:n], 1.0)
+    ob, lb = ref.attend_bounds(r, v, idx[:n], torch.bfloat16)
+    assert bool(((out[:n].double() - r["out"]).abs() <= ob).all())
+    assert bool(((lse[:n].double() - r["lse"]).abs() <= lb).all())
