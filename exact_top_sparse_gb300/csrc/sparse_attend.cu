@@ -172,11 +172,12 @@ __device__ __noinline__ void look_up_rows(const Args* a, int32_t t, int32_t hk, 
   }
 }
 
-// NC: key columns of a tile per row copy (128 / copies).  BENT: a cap or a bias.
+// NC: key columns of a tile per row copy (128 / copies).  BENT: 1 a cap or a bias, 2 a cap
+// above WIDE_CAP (a branch in one kernel instead took 288 us for 270).
 // Chunks of 32 columns run in loops, not unrolled: five kinds of warps share the
 // instruction cache, and 64 columns held in registers took longer than 32 read
 // twice.
-template <int D, int NC, bool BF16, bool BENT>
+template <int D, int NC, bool BF16, int BENT>
 __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ Args a) {
   using P = Plan<D>;
   constexpr int PER = NC;  // rows per copy: with R = 128 / NC copies, 128 / R rows
@@ -300,7 +301,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_attend(const __grid_constant__ A
       // 32 raw products -> base-2 logits, where that takes more than a factor
       auto finish = [&](float (&x)[32], int at) {
         if (BENT) {
-          if (a.cap > 0.0f) {
+          if (BENT == 2) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = cap_out * tanh_near(x[i] * cap_in);
+          } else if (a.cap > 0.0f) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = cap_out * tanh_of(x[i] * cap_in);
           } else {
@@ -935,7 +939,7 @@ int check_args(const Args& a, int32_t D, int32_t dtype) {
   return TOPK_OK;
 }
 
-template <int D, int NC, bool BF16, bool BENT>
+template <int D, int NC, bool BF16, int BENT>
 int launch_kernel(const Args& a, int C, int sms, cudaStream_t st) {
   static OncePerDevice opted_in;
   int dev = 0;
@@ -961,7 +965,7 @@ int launch_kernel(const Args& a, int C, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k_attend<D, NC, BF16, BENT>, a) == cudaSuccess ? TOPK_OK : TOPK_ERR_CUDA;
 }
 
-template <int D, bool BF16, bool BENT>
+template <int D, bool BF16, int BENT>
 int launch_rows(const Args& a, int C, int sms, cudaStream_t st) {
   if (a.G <= 32) return launch_kernel<D, 32, BF16, BENT>(a, C, sms, st);
   if (a.G <= 64) return launch_kernel<D, 64, BF16, BENT>(a, C, sms, st);
@@ -970,8 +974,9 @@ int launch_rows(const Args& a, int C, int sms, cudaStream_t st) {
 
 template <int D, bool BF16>
 int launch_bent(const Args& a, int C, int sms, cudaStream_t st) {
-  return a.cap > 0.0f || a.slopes ? launch_rows<D, BF16, true>(a, C, sms, st)
-                                  : launch_rows<D, BF16, false>(a, C, sms, st);
+  return a.cap > WIDE_CAP              ? launch_rows<D, BF16, 2>(a, C, sms, st)
+         : a.cap > 0.0f || a.slopes ? launch_rows<D, BF16, 1>(a, C, sms, st)
+                                    : launch_rows<D, BF16, 0>(a, C, sms, st);
 }
 
 // CTAs per item: the split with the least rounds of (chunks + one for the

@@ -248,7 +248,14 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
             tc::tm_ld32(td + c, ud);
             tc::wait_ld();
             float x[32];
-            if (a.cap > 0.0f) {
+            if (a.cap > WIDE_CAP) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float th = tanh_near(us[i] * cap_in);
+                x[i] = cap_out * th;
+                ud[i] = fmaf(ud[i], times, less) * fmaf(-th, th, 1.0f);
+              }
+            } else if (a.cap > 0.0f) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float th = tanh_of(us[i] * cap_in);

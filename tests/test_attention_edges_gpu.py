@@ -202,3 +202,23 @@ def test_large_and_small_values_under_growing_scores(ets, T, H, power):  # noqa:
     ob, lb = ref.attend_bounds(r, v, idx[:n], torch.bfloat16)
     assert bool(((out[:n].double() - r["out"]).abs() <= ob).all())
     assert bool(((lse[:n].double() - r["lse"]).abs() <= lb).all())
+
+
+@pytest.mark.parametrize("softcap", [300.0, 1e4, 1e6, 1e30])
+@pytest.mark.parametrize("H", [8, 100])
+def test_caps_far_above_the_scores(ets, softcap, H):  # noqa: F811
+    """Such a cap changes next to nothing: its tanh is right relative to the score
+    (2^-20 of it: below the product's own bound), not only to the cap."""
+    T, D, K, S = 6, 64, 200, 400
+    q, k, v, idx = _inputs(T, H, 1, D, K, S)
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, softcap=softcap, return_lse=True)
+    r = ref.attend(q, k, v, idx, D ** -0.5, softcap)
+    r["mag"] = ref.attend(q, k, v, idx, D ** -0.5)["mag"]  # without what a cap may add
+    ob, lb = ref.attend_bounds(r, v, idx, q.dtype)
+    assert bool(((out.double() - r["out"]).abs() <= ob).all())
+    assert bool(((lse.double() - r["lse"]).abs() <= lb).all())
+    dout = _rand(q.shape, q.dtype, 7)
+    got = ets.topk_sparse_attention_backward(dout, q, k, v, idx, out, lse, softcap=softcap)
+    want, bound = ref.attend_grad(dout, q, k, v, idx, out, lse, r, D ** -0.5, softcap)
+    for g, w, b in zip(got, want, bound):
+        assert bool(((g.double() - w).abs() <= b).all())
