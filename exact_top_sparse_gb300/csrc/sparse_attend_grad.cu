@@ -228,7 +228,10 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
       const int64_t at = (int64_t)t * a.H + hk * a.G + h;
       const float slope = a.slopes && live ? a.slopes[hk * a.G + h] * LOG2E : 0.0f;
       const int32_t pos = a.slopes ? a.pos[t] : 0;
-      const float lse = live ? a.lse_in[at] * LOG2E : INFINITY;  // p = 0 in rows of no head
+      // p = 0 in rows of no head, and where no key is left or all scores are -inf
+      // (lse = -inf: 2^(-inf + inf) would be NaN)
+      float lse = live ? a.lse_in[at] * LOG2E : INFINITY;
+      if (lse == -INFINITY) lse = INFINITY;
       const float delta = live ? a.delta[at] : 0.0f;
       for (;;) {
         const uint32_t is = ti % G_NI;

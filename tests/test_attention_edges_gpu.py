@@ -222,3 +222,25 @@ def test_caps_far_above_the_scores(ets, softcap, H):  # noqa: F811
     want, bound = ref.attend_grad(dout, q, k, v, idx, out, lse, r, D ** -0.5, softcap)
     for g, w, b in zip(got, want, bound):
         assert bool(((g.double() - w).abs() <= b).all())
+
+
+@pytest.mark.parametrize("H", [4, 40, 100])
+def test_gradients_of_rows_whose_scores_are_all_minus_infinity(ets, H):  # noqa: F811
+    """A bias below every finite score leaves nothing: out 0, lse -inf, gradients 0."""
+    T, D, K, S = 5, 64, 150, 400
+    q, k, v, idx = _inputs(T, H, 1, D, K, S)
+    slopes = torch.zeros(H, device=DEV)
+    slopes[1] = 2e38
+    opt = {"slopes": slopes, "positions": torch.full((T,), 2000, dtype=torch.int32, device=DEV)}
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, return_lse=True, **opt)
+    assert float(out[:, 1].float().abs().max()) == 0.0 and bool((lse[:, 1] == -math.inf).all())
+    dout = _rand(q.shape, q.dtype, 7)
+    dq, dk, dv = ets.topk_sparse_attention_backward(dout, q, k, v, idx, out, lse, **opt)
+    assert float(dq[:, 1].float().abs().max()) == 0.0
+    keep = [h for h in range(H) if h != 1]
+    plain = [t[:, keep].contiguous() for t in (dout, q, out)]
+    _, ek, ev = ets.topk_sparse_attention_backward(plain[0], plain[1], k, v, idx, plain[2],
+                                                   lse[:, keep].contiguous())
+    for a, b in ((dk, ek), (dv, ev)):
+        assert bool(a.isfinite().all())
+        assert float((a.double() - b.double()).abs().max()) <= 2.0 ** -7 * float(b.abs().max())
