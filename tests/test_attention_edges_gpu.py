@@ -244,3 +244,38 @@ def test_gradients_of_rows_whose_scores_are_all_minus_infinity(ets, H):  # noqa:
     for a, b in ((dk, ek), (dv, ev)):
         assert bool(a.isfinite().all())
         assert float((a.double() - b.double()).abs().max()) <= 2.0 ** -7 * float(b.abs().max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,H,Hk,D", [(2, 128, 4, 64), (24, 128, 1, 64), (7, 32, 8, 128), (300, 8, 1, 128)])
+def test_rows_with_one_key(ets, dtype, T, H, Hk, D):  # noqa: F811
+    """One key: out is its value, dv its dout, and dq and dk are zero up to the
+    rounding of dP - delta, two sums of the same D products: 2 D 2^-24 of their
+    magnitudes each (4 where an accumulator truncates), times the scale and the
+    other factor."""
+    S = 500
+    q, k, v, idx = _inputs(T, H, Hk, D, 17, S, dtype, fill=[t % 2 for t in range(T)])
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, return_lse=True)
+    dout = _rand(q.shape, dtype, 7)
+    dq, dk, dv = ets.topk_sparse_attention_backward(dout, q, k, v, idx, out, lse)
+    G, scale = H // Hk, D ** -0.5
+    slack = torch.zeros((S, Hk, D), dtype=torch.float64, device=DEV)
+    sums = torch.zeros_like(slack)
+    for t in range(T):
+        if t % 2 == 0:
+            assert not bool(out[t].any()) and not bool(dq[t].any())
+            continue
+        key = int(idx[t].max())
+        vh, kh = (x[key].repeat_interleave(G, 0) for x in (v, k))
+        assert torch.equal(out[t], vh)
+        res = 4 * 2 * D * 2.0 ** -24 * (dout[t].double() * vh.double()).abs().sum(-1) * scale  # [H]
+        tiny = 2.0 ** -24 if dtype == torch.float16 else 0.0
+        assert bool((dq[t].double().abs() <= res[:, None] * 1.01 * kh.double().abs() + tiny).all())
+        slack[key] += (res[:, None] * q[t].double().abs()).view(Hk, G, D).sum(1)
+        sums[key] += dout[t].double().view(Hk, G, D).sum(1)
+    assert bool((dk.double().abs() <= 1.01 * slack + (2.0 ** -24 if dtype == torch.float16 else 0)).all())
+    # P is 1 to FP32's exponential and logarithm (2^-20), rounded to 16 bits: 1
+    mag = torch.zeros_like(sums)
+    for t in range(1, T, 2):
+        mag[int(idx[t].max())] += dout[t].double().abs().view(Hk, G, D).sum(1)
+    assert bool(((dv.double() - sums).abs() <= ref.rounding(sums, dtype) + 2.0 ** -18 * mag).all())
