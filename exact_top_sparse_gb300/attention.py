@@ -8,7 +8,10 @@ gradients (CUDA, sm_103a; C entry points in include/topk.h).
     out = ets.topk_sparse_attention(q, k_cache, v_cache, idx)
 
 The calls run on `stream` (default: the current stream of the tensors' device),
-return without waiting and can be captured in a CUDA graph.  They do not
+return without waiting and can be captured in a CUDA graph.  On another stream
+than the current one they take their memory from it and keep the inputs' until
+it has passed; that the inputs are complete there, and the results before they
+are read here, is for the caller to wait for.  They do not
 record a graph for autograd: the gradients are calls of their own
 (topk_rope(..., inverse=True), topk_qk_norm_rope_backward,
 topk_sparse_attention_backward).  Like the rest of the package they have no CPU
@@ -106,10 +109,22 @@ def _result(name, out, like, stream):
 
 
 def _new(shape, dtype, like, stream):
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)  # allocated on the current stream, used on `stream`
+    """A result or a workspace of a call on `stream`.  Its memory is that stream's: a
+    block of the current stream's may still be in use by work queued there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))  # where the caller reads it
     return t
+
+
+def _used_on(stream, *tensors):
+    """Inputs of a call on another stream: their memory is not handed on before it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _call(name, index, stream, *args):
@@ -210,6 +225,7 @@ def topk_rope(x, positions, freqs, interleaved: bool = False, offset: int = 0, s
     out = _result("out", out, x, stream)
     _call("topk_rope", index, stream, *xp, *_heads("out", out, _CODE), T, H, D, _CODE[x.dtype],
           *turn, inverse, scale)
+    _used_on(stream, x, positions, freqs)
     return out
 
 
@@ -242,6 +258,7 @@ def topk_qk_norm_rope(q, k, q_weight, k_weight, positions, freqs, interleaved: b
     _call("topk_qk_norm_rope", index, stream, *qp, H, *kp, k.shape[1], qw, kw, w32,
           *_heads("q_out", q_out, _CODE), *_heads("k_out", k_out, _CODE), T, D, _CODE[q.dtype],
           *turn, scale, eps)
+    _used_on(stream, q, k, q_weight, k_weight, positions, freqs)
     return q_out, k_out
 
 
@@ -265,6 +282,7 @@ def topk_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positio
     _call("topk_qk_norm_rope_backward", index, stream, *dqp, *dkp, *qp, H, *kp, k.shape[1], qw, kw,
           w32, T, D, _CODE[q.dtype], *turn, scale, eps, dq.data_ptr(), dk.data_ptr(),
           at if qw else None, at + 4 * D if kw else None, at + 8 * D, 4 * n)
+    _used_on(stream, dq_out, dk_out, q, k, q_weight, k_weight, positions, freqs)
     dqw, dkw = w[:D] if qw else None, w[D:2 * D] if kw else None
     return dq, dk, dqw, dkw
 
@@ -326,6 +344,7 @@ def topk_sparse_attention(q, k, v, idx, scale: float = None, softcap: float = 0.
     _call("topk_sparse_attention", index, stream, *qp, *kp, *vp, *rows, T, k.shape[0], H,
           k.shape[1], D, K, _CODE[q.dtype], scale, softcap, *mask, out.data_ptr(),
           lse.data_ptr() if return_lse else None)
+    _used_on(stream, q, k, v, idx, slopes, positions, key_lo, key_hi)
     return (out, lse) if return_lse else out
 
 
@@ -357,6 +376,7 @@ def topk_sparse_attention_backward(dout, q, k, v, idx, out, lse, scale: float = 
     _call("topk_sparse_attention_backward", index, stream, *dp, *qp, *kp, *vp, *rows,
           out.data_ptr(), lse.data_ptr(), T, S, H, Hk, D, K, _CODE[q.dtype], scale, softcap, *mask,
           dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), w.data_ptr(), n)
+    _used_on(stream, dout, q, k, v, idx, out, lse, slopes, positions, key_lo, key_hi)
     if kv_dim == 2:
         dk, dv = dk.squeeze(1), dv.squeeze(1)
     return dq, dk, dv

@@ -279,3 +279,62 @@ def test_rows_with_one_key(ets, dtype, T, H, Hk, D):  # noqa: F811
     for t in range(1, T, 2):
         mag[int(idx[t].max())] += dout[t].double().abs().view(Hk, G, D).sum(1)
     assert bool(((dv.double() - sums).abs() <= ref.rounding(sums, dtype) + 2.0 ** -18 * mag).all())
+
+
+def test_results_on_another_stream_wait_for_nobody(ets):  # noqa: F811
+    """A call on another stream takes its memory from that stream: blocks that the
+    current stream still uses are not written into."""
+    T, H, D, K, S = 64, 16, 128, 300, 900
+    q, k, v, idx = _inputs(T, H, 1, D, K, S)
+    dout, x = _rand(q.shape, q.dtype, 7), _rand((T, 1, D), q.dtype, 8)
+    w, pos = torch.ones(D, device=DEV), torch.arange(T, dtype=torch.int32, device=DEV)
+    freqs = ets.rope_freqs(D)
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, return_lse=True)
+
+    def calls(stream=None):
+        return (*ets.topk_sparse_attention(q, k, v, idx, return_lse=True, stream=stream),
+                ets.topk_sparse_attention_backward(dout, q, k, v, idx, out, lse, stream=stream)[0],
+                ets.topk_rope(q, pos, freqs, stream=stream),
+                *ets.topk_qk_norm_rope(q, x, w, w, pos, freqs, stream=stream),
+                *ets.topk_qk_norm_rope_backward(dout, x, q, x, w, w, pos, freqs, stream=stream))
+
+    want = calls()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    # blocks of every size that the calls ask for, still to be written by this stream
+    late = [torch.empty_like(t) for t in want for _ in range(4)]
+    late += [torch.empty(n, dtype=torch.uint8, device=DEV) for n in (1 << 17, 1 << 19, 1 << 20, 1 << 21)]
+    for t in late:  # (loads the kernels)
+        t.fill_(6)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    for t in late:
+        t.fill_(7)
+    del late, t
+    got = calls(s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_inputs_of_another_stream_outlive_the_call(ets):  # noqa: F811
+    """The caller may drop the inputs as soon as a call on another stream returns."""
+    T, H, D, K, S = 64, 16, 128, 300, 900
+    base = _inputs(T, H, 1, D, K, S)
+    want = ets.topk_sparse_attention(*base)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    mine = [t.clone() for t in base]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    got = ets.topk_sparse_attention(*mine, stream=s)
+    shapes = [(t.shape, t.dtype) for t in mine]
+    del mine
+    over = [torch.full(sh, 3, dtype=dt, device=DEV) for sh, dt in shapes for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    del over
