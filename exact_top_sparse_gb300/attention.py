@@ -291,7 +291,7 @@ def topk_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positio
 _I32_ONLY, _F32_ONLY = (torch.int32,), (torch.float32,)
 
 
-def _selection(q, k, v, idx, scale, slopes, positions, key_lo, key_hi):
+def _selection(q, k, v, idx, scale, slopes, positions, key_lo, key_hi, stream):
     qp = _heads("q", q, _NARROW_CODE)
     if isinstance(k, torch.Tensor) and k.dim() == 2:
         k = k.unsqueeze(1)  # [S, D]: one key head
@@ -310,13 +310,17 @@ def _selection(q, k, v, idx, scale, slopes, positions, key_lo, key_hi):
         raise TypeError("idx must be an int32 [T, K] tensor with unit stride in K on q's device")
     if slopes is not None and positions is None:
         raise TypeError("positions is required with slopes")
+    if idx.shape[1] == 0:  # nothing selected anywhere: one entry that is skipped
+        idx = _new((T, 1), torch.int32, q, stream)
+        with torch.cuda.stream(stream):
+            idx.fill_(-1)
     K = idx.shape[1]
     mask = (_vector("slopes", slopes, _F32_ONLY, H, index),
             _vector("positions", positions, _I32_ONLY, T, index),
             _vector("key_lo", key_lo, _I32_ONLY, T, index),
             _vector("key_hi", key_hi, _I32_ONLY, T, index))
     rows = (idx.data_ptr(), idx.stride(0) if T > 1 else K)
-    return k, v, qp, kp, vp, rows, K, D ** -0.5 if scale is None else scale, mask, index
+    return k, v, idx, qp, kp, vp, rows, K, D ** -0.5 if scale is None else scale, mask, index
 
 
 def topk_sparse_attention(q, k, v, idx, scale: float = None, softcap: float = 0.0, slopes=None,
@@ -325,17 +329,18 @@ def topk_sparse_attention(q, k, v, idx, scale: float = None, softcap: float = 0.
     """Attention of every query token over its selected keys.
 
     q [T, H, D], k and v [S, Hk, D] (or [S, D]: one key head for all), bfloat16
-    or float16, D 64 or 128, H a multiple of Hk, at most 128 query heads to a key
-    head; any token and head strides that are multiples of 8.  idx [T, K] int32:
-    slots of k and v, as topk_ragged writes them; -1 and anything outside [0, S)
-    is skipped.  Options: softcap c (> 0) puts c * tanh(z / c) in the place of
+    or float16, D 64 or 128, H a multiple of Hk, at most 128 query heads to a
+    key head; any token and head strides that are multiples of 8. idx [T, K]
+    int32: slots of k and v, as topk_ragged writes them; -1 and anything
+    outside [0, S) is skipped (rows one after another, or one row expanded to
+    all tokens). Options: softcap c (> 0) puts c * tanh(z / c) in the place of
     the scaled score z; slopes [H] float32 subtract slopes[h] * |positions[t] -
-    i|; key_lo, key_hi [T] int32 keep only key_lo[t] <= i < key_hi[t] (documents,
-    prefixes).  A token that has no key left gets 0.
+    i|; key_lo, key_hi [T] int32 keep only key_lo[t] <= i < key_hi[t]
+    (documents, prefixes). A token that has no key left gets 0.
 
     Returns out [T, H, D], or (out, lse [T, H] float32) with return_lse."""
-    k, v, qp, kp, vp, rows, K, scale, mask, index = _selection(q, k, v, idx, scale, slopes,
-                                                               positions, key_lo, key_hi)
+    k, v, idx, qp, kp, vp, rows, K, scale, mask, index = _selection(
+        q, k, v, idx, scale, slopes, positions, key_lo, key_hi, stream)
     T, H, D = q.shape
     out = _result("out", out, q, stream)
     if not out.is_contiguous():
@@ -357,8 +362,8 @@ def topk_sparse_attention_backward(dout, q, k, v, idx, out, lse, scale: float = 
     order and rounded once."""
     dp = _heads("dout", dout, _NARROW_CODE, q)
     kv_dim = k.dim() if isinstance(k, torch.Tensor) else 0
-    k, v, qp, kp, vp, rows, K, scale, mask, index = _selection(q, k, v, idx, scale, slopes,
-                                                               positions, key_lo, key_hi)
+    k, v, idx, qp, kp, vp, rows, K, scale, mask, index = _selection(
+        q, k, v, idx, scale, slopes, positions, key_lo, key_hi, stream)
     T, H, D = q.shape
     if dout.shape != q.shape:
         raise TypeError("dout must have q's shape")

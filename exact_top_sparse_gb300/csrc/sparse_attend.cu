@@ -921,7 +921,7 @@ int device_sms(int* sms) {
 }
 
 int check_args(const Args& a, int32_t D, int32_t dtype) {
-  if (a.T < 0 || a.H < 1 || a.Hk < 1 || a.K < 1 || a.S < 0 || a.ld_idx < a.K ||
+  if (a.T < 0 || a.H < 1 || a.Hk < 1 || a.K < 1 || a.S < 0 || (a.ld_idx < a.K && a.ld_idx != 0) ||
       (int64_t)a.T * a.H > INT32_MAX || !(a.scale > 0.0f) || !std::isfinite(a.scale) ||
       !std::isfinite(a.cap) || a.k_ts < 0 || a.k_ts > INT32_MAX || a.v_ts < 0 ||
       a.v_ts > INT32_MAX)

@@ -476,7 +476,8 @@ int topk_qk_norm_rope_backward(
  * position + 1), [0, max(position + 1, prefix length)).
  *   q          device, [T][H][D]; k, v: device, [S][Hk][D]; unit stride in D,
  *              strides in elements, multiples of 8; 16-byte aligned
- *   idx        device, [T][ld_idx] int32, the first K of every row are read
+ *   idx        device, [T][ld_idx] int32, the first K >= 1 of every row are read;
+ *              ld_idx >= K, or 0: one row for all tokens
  *   dtype      TOPK_BF16 or TOPK_FP16 for q, k, v and out
  *   D          64 or 128; H a multiple of Hk, H / Hk <= 128 (else
  *              TOPK_ERR_UNSUPPORTED_SHAPE); T * H < 2^31

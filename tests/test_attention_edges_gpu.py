@@ -338,3 +338,29 @@ def test_inputs_of_another_stream_outlive_the_call(ets):  # noqa: F811
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     del over
+
+
+@pytest.mark.parametrize("T", [0, 1, 5])
+def test_no_selected_keys_at_all(ets, T):  # noqa: F811
+    """idx with no column: nothing is left in any row."""
+    q, k, v, _ = _inputs(T, 8, 2, 64, 1, 30)
+    idx = torch.empty((T, 0), dtype=torch.int32, device=DEV)
+    out, lse = ets.topk_sparse_attention(q, k, v, idx, return_lse=True)
+    assert out.shape == q.shape and not bool(out.any()) and bool((lse == -math.inf).all())
+    grads = ets.topk_sparse_attention_backward(_rand(q.shape, q.dtype, 7), q, k, v, idx, out, lse)
+    assert [g.shape for g in grads] == [q.shape, k.shape, v.shape]
+    assert not any(bool(g.any()) for g in grads)
+
+
+def test_one_row_of_keys_for_all_tokens(ets):  # noqa: F811
+    """idx broadcast over the tokens (row stride 0)."""
+    q, k, v, idx = _inputs(9, 8, 2, 64, 200, 300)
+    row = idx[:1].expand(9, -1)
+    assert row.stride(0) == 0
+    dout = _rand(q.shape, q.dtype, 7)
+    out, lse = ets.topk_sparse_attention(q, k, v, row, return_lse=True)
+    want, wlse = ets.topk_sparse_attention(q, k, v, row.contiguous(), return_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    a = ets.topk_sparse_attention_backward(dout, q, k, v, row, out, lse)[0]
+    b = ets.topk_sparse_attention_backward(dout, q, k, v, row.contiguous(), out, lse)[0]
+    assert torch.equal(a, b)
