@@ -105,6 +105,8 @@ def _result(name, out, like, stream):
     if not (isinstance(out, torch.Tensor) and out.get_device() == like.get_device()
             and out.dtype == like.dtype and out.shape == like.shape):
         raise TypeError("%s must have the input's shape, element type and device" % name)
+    if 0 in out.stride() and any(n > 1 and s == 0 for n, s in zip(out.shape, out.stride())):
+        raise ValueError("%s must not overlap itself (expanded dimensions)" % name)
     return out
 
 

@@ -364,3 +364,16 @@ def test_one_row_of_keys_for_all_tokens(ets):  # noqa: F811
     a = ets.topk_sparse_attention_backward(dout, q, k, v, row, out, lse)[0]
     b = ets.topk_sparse_attention_backward(dout, q, k, v, row.contiguous(), out, lse)[0]
     assert torch.equal(a, b)
+
+
+def test_outputs_that_overlap_themselves_are_refused(ets):  # noqa: F811
+    """An expanded tensor as output would be written by many rows."""
+    pos, freqs = torch.arange(4, dtype=torch.int32, device=DEV), ets.rope_freqs(64)
+    x = _rand((4, 8, 64), torch.bfloat16)
+    for out in (x[:1].expand(4, -1, -1), x[:, :1].expand(-1, 8, -1)):
+        out = out.to(x.dtype)
+        assert 0 in out.stride()
+        with pytest.raises(ValueError, match="overlap"):
+            ets.topk_rope(x, pos, freqs, out=out)
+        with pytest.raises(ValueError, match="overlap"):
+            ets.topk_qk_norm_rope(x, x, None, None, pos, freqs, q_out=out)
