@@ -281,6 +281,32 @@ def test_rows_with_one_key(ets, dtype, T, H, Hk, D):  # noqa: F811
     assert bool(((dv.double() - sums).abs() <= ref.rounding(sums, dtype) + 2.0 ** -18 * mag).all())
 
 
+def _rounds(ets_, T, H, Hk, D, K, S, fill, dtype=torch.bfloat16):
+    q, k, v, idx = _inputs(T, H, Hk, D, K, S, dtype, fill=fill)
+    out, lse = ets_.topk_sparse_attention(q, k, v, idx, return_lse=True)
+    for a in range(0, T, 4):
+        b = min(a + 4, T)
+        r = ref.attend(q[a:b], k, v, idx[a:b], D ** -0.5)
+        ob, lb = ref.attend_bounds(r, v, idx[a:b], dtype)
+        assert bool(((out[a:b].double() - r["out"]).abs() <= ob).all())
+        none = torch.isinf(r["lse"])
+        assert torch.equal(torch.isinf(lse[a:b]), none)
+        assert bool(((lse[a:b].double() - r["lse"]).abs() <= lb)[~none].all())
+    assert ets_.sparse_attention_read_status() == 0
+
+
+# a little more items than SMs (or than SMs / 4) and many chunks: clusters of 2, 4
+# and 8 CTAs with several items each, an odd last round among them
+@pytest.mark.parametrize("D,G,Hk", [(64, 8, 8), (128, 8, 1), (128, 64, 4), (64, 128, 8), (128, 100, 5)])
+@pytest.mark.parametrize("K,items", [(2048, 1.05), (2048, 1.3), (4096, 1.05), (8000, 0.3)])
+def test_clusters_with_several_items(ets, D, G, Hk, K, items):  # noqa: F811
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    T = -(-int(sms * items) // Hk)
+    # rows that leave CTAs of a cluster without a tile, empty rows, full ones
+    fill = [(K, 0, 100, K - 1, 129, 1, K)[t % 7] for t in range(T)]
+    _rounds(ets, T, G * Hk, Hk, D, K, 9000, fill)
+
+
 def test_results_on_another_stream_wait_for_nobody(ets):  # noqa: F811
     """A call on another stream takes its memory from that stream: blocks that the
     current stream still uses are not written into."""
