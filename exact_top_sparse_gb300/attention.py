@@ -24,8 +24,6 @@ import torch
 
 from exact_top_sparse_gb300 import _check, load_library
 
-ROPE_MAX_DIM = 512
-
 _VP, _I64, _I32, _F, _SZ = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
                             ctypes.c_size_t)
 _HEADS = [_VP, _I64, _I64]                      # pointer, token stride, head stride
