@@ -25,9 +25,10 @@
 //
 // Measured on GB300 (BF16, in a graph): rotation of 8192 x 64 x 128 44 us (6.1
 // TB/s, 0.90 of the measured copy rate), norm + rotation of 16384 x 36 x 128 63 us
-// (4.8 TB/s; instructions bound it, two elements in each), its gradient of 8192 x
-// 40 x 128 63 us (4.0 TB/s; two sums over the row between its loads and its
-// stores), one token 2.8 us.  Rows on their way through a ring of asynchronous
+// (4.8 TB/s; instructions bound it, two elements in each, and at the 64 registers of
+// four blocks an SM the BF16 kernel spills 246 bytes a thread), its gradient of 8192 x
+// 40 x 128 61 us (4.1 TB/s; two sums over the row between its loads and its stores,
+// and 118 bytes spilled at 80 registers), one token 2.5 us.  Rows on their way through a ring of asynchronous
 // copies in shared memory cost instructions and brought nothing (gradient 93 us
 // with it and 94 without, before its blocks were balanced).
 #include <cuda_bf16.h>
@@ -45,7 +46,8 @@ namespace tr {
 
 constexpr int THREADS = 256;
 constexpr int MAX_D = 512;
-constexpr int MAX_BLOCKS = 456;  // of the backward pass, three per SM: rows of partial sums of dw
+constexpr int MAX_BLOCKS = 456;  // of the backward pass, three for each of 152 SMs (rows of
+                                 // partial sums of dw)
 constexpr int TABLE_COST = 4;    // passes over the table to the time of a round of rows
 
 struct Side {
@@ -496,7 +498,7 @@ int launch(Args& a, int64_t T, int32_t dtype, int mode, cudaStream_t st) {
   // Tokens of a block at a time: about 8 rows to a group (the gradient: 4, of its
   // side), the count near that whose rows fill the groups best, at most 16 KB of
   // sines and cosines (a block's rows also stay below 2^16, for inv_h), and fewer
-  // while that leaves SMs without two blocks.
+  // while that leaves some of 152 SMs without two blocks.
   const int per_block = THREADS / L;
   const int H0 = a.side[0].H, H1 = a.side[1].H;
   auto rounds = [&](int64_t t, int h) { return (t * h + per_block - 1) / per_block; };

@@ -8,8 +8,8 @@
 // Every token has keys of its own, so a key row is read once per token and
 // key head, and serves the G = H / Hk query heads that share it: G flops for
 // every byte gathered.  Measured on GB300: 2048 queries x 64 heads x 128 with
-// Top-2048 of a 128K cache 252 us (137 GFLOP: 546 TFLOP/s; 2.1 GB gathered: 8.5
-// TB/s), 1024 x 128 heads 125-129 us (1.06-1.10 PFLOP/s), one token 14 us in a
+// Top-2048 of a 128K cache 247 us (137 GFLOP: 556 TFLOP/s; 2.1 GB gathered: 8.7
+// TB/s), 1024 x 128 heads of an 8K cache 124 us (1.11 PFLOP/s), one token 14 us in a
 // graph.  A plain kernel gathers random 256-byte rows out of L2 at 20 TB/s (8.7
 // with cp.async by 128 threads of an SM, 14 by 256; gather4 tensor copies issued
 // by one warp reached 2.4), and the products of a tile take 1024 cycles; a tile

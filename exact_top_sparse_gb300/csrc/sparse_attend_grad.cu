@@ -16,13 +16,13 @@
 // vector reductions to global memory: 8 D bytes per token, key and key head,
 // against 4 D gathered.  Those bound the kernel, not the tensor core: on GB300 a
 // kernel that does nothing else reaches 6.3 TB/s of reductions into 8 MB (L2), and
-// this one 4.4-4.5 (1024 queries x 64 heads x 128, Top-2048 of 8192: 489 us, of
+// this one 4.4-4.5 (1024 queries x 64 heads x 128, Top-2048 of 8192: 492 us, of
 // them 341 us at that rate).  Without the reductions a tile takes 6700 cycles
 // instead of 8400, without their way through tensor and shared memory 6000.  Their
 // order is the scheduler's, so the sums differ by FP32 rounding between runs.
 // P and dS are rounded to the inputs' 16-bit type before the last three products
 // (the tensor core takes no wider operand beside 16-bit values; the error against
-// 64 bits is 1.1 to 1.4 times that of FP32 products).  dS leaves the scale out until
+// 64 bits is 1.1 to 1.3 times that of FP32 products).  dS leaves the scale out until
 // the FP32 results, and in FP16 it is held times a power of two that brings the
 // item's largest |dout| into [4, 8) and is taken out of those results, exactly: with a
 // scaled loss dS itself passes 65504 where dq, dk and dv do not.  8 (|v|_1 + |out|_1)
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_attend_grad(const __grid_const
       bool any = false;
       float undo = a.scale;  // dS's factor out of the results, and the scale in
       // an infinite or NaN dout leaves its mark in delta; without one dV needs no look
-      // (looking at every row of dV took 615 us for 493 with 1024 x 64 heads x 128)
+      // (looking at every row of dV took 615 us for 492 with 1024 x 64 heads x 128)
       bool mark = false;
       for (int32_t h = (int32_t)lane; h < a.G; h += 32)
         mark |= !(fabsf(a.delta[(int64_t)t * a.H + hk * a.G + h]) < INFINITY);

@@ -487,6 +487,8 @@ int topk_qk_norm_rope_backward(
  *              [T][H] float, or NULL
  * Products of 16-bit values, FP32 sums; the softmax weights are rounded to the
  * 16-bit type for the second product.  The result does not depend on the run.
+ * A NaN score makes its row of out and lse NaN, with a softcap too; an infinite
+ * value of a selected key gives that infinity (NaN where both signs meet).
  * One launch on `stream`, no workspace.  A bounded internal wait that gives up
  * sets TOPK_FLAG_TIMEOUT in the word topk_sparse_attention_read_status()
  * returns (and clears; it syncs the stream). */
